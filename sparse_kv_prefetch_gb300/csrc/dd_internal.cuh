@@ -315,6 +315,12 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity,
     if (global_ns() - t0 > kWaitLimitNs) return false;
   return true;
 }
+// Order this thread's ordinary accesses of shared memory, reads and writes, before
+// what the async proxy (bulk copies, tcgen05) does there once it is told of them:
+// its reads of what was written, and its writes over what was read.
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 // global -> shared, completion counted on `bar` (bytes and addresses 16-aligned).
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gmem_src, uint32_t bytes,
                                           uint64_t* bar) {

@@ -188,6 +188,16 @@ __global__ void __launch_bounds__(kScoreThreads, use_mma<T, G, QB>() && !FUSED ?
   int head0 = -1;
   bool ok = true;
   const unsigned char* Ku = K + (size_t)u * n * RB;
+  // A consumer warp is done with stage s: it may be refilled.  The refill is a
+  // write of the async proxy, and an arrival alone does not hold it back until the
+  // warp's loads from the stage have been served: beside another kernel that keeps
+  // the SM's load/store unit busy they are still queued, and would read the keys
+  // of four stages later.
+  auto release = [&](int s) {
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+  };
 
   if (warp == kConsumerWarps) {
     // Producer: one lane keeps up to kStages bulk copies in flight.
@@ -268,8 +278,7 @@ __global__ void __launch_bounds__(kScoreThreads, use_mma<T, G, QB>() && !FUSED ?
           mma_16x8x16(acc, a0.z, a1.z, a0.w, a1.w, qb[bb].z, qb[bb].w);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);  // the stage may be refilled
+      release(s);
       if (mine && head0 >= 0) {
         const int j0 = j_begin + t * SR + par * HALF + tau * 8 + hr;  // mma row g
         const int j1 = j0 + 4;                                          // mma row g + 8
@@ -375,8 +384,7 @@ __global__ void __launch_bounds__(kScoreThreads, use_mma<T, G, QB>() && !FUSED ?
           acc[g * RPG + i + 1] = sum.y;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);  // the stage may be refilled
+      release(s);
       // Transposed reduction over the LPR lanes of the group: at step t each
       // lane keeps the lower half of its slots, sends the upper half to the
       // lane 2^t away and adds what it receives.

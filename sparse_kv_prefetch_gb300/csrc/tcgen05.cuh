@@ -32,10 +32,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-// Make ordinary shared-memory writes visible to the async proxy (TMA, tcgen05).
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
+using dd::fence_async_smem;
 
 // -------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor for the 128-byte swizzle: bits 0-13 the
