@@ -133,6 +133,15 @@ __device__ __forceinline__ float code_16(uint32_t w, int i) {
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
+// A wait that lasts as long as other roles' work, which grows with the number of
+// keys: it ends with that work, or when a role whose waits are for single tiles
+// (two seconds each) has given up and says so.
+__device__ __forceinline__ bool wait_for_roles(uint64_t* bar, uint32_t parity,
+                                               const uint32_t* failed) {
+  for (uint32_t n = 0; !mbar_try_wait_sleep(bar, parity, 1000); ++n)
+    if (*const_cast<const volatile uint32_t*>(failed) != 0 || n >= (1u << 30)) return false;
+  return true;
+}
 
 template <int D, int NT, int BN, bool Q4>
 __global__ void __launch_bounds__(Roles<Q4>::kThreads, 1)
@@ -217,11 +226,11 @@ __global__ void __launch_bounds__(Roles<Q4>::kThreads, 1)
           return;
         }
       }
-      if constexpr (decltype(single)::value) {
-        if (!(ok = mbar_wait(&bars.given, phase))) return;
-      } else {
-        if (!(ok = wait_all(&bars.given, phase))) return;
-      }
+      // A role without work in its last places (a row tile without rows) waits here
+      // for those of the others.
+      ok = wait_for_roles(&bars.given, phase, &bars.failed);
+      if constexpr (!decltype(single)::value) ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
       const bool more = tc::work_given(&bars.answer, x, y, z);
       tc::fence_async_smem();  // read before the next answer is written
       if constexpr (decltype(single)::value) {
@@ -269,12 +278,9 @@ __global__ void __launch_bounds__(Roles<Q4>::kThreads, 1)
         if (!(ok = mbar_wait(&bars.given, phase))) break;
         int x, y, z;
         if (!tc::work_given(&bars.answer, x, y, z)) break;
-        // Not asked again before every role has gone on to this one.  That takes as
-        // long as the work before it, so this wait ends with them or when one of
-        // them, whose own waits are all for single tiles, gives up.
-        for (uint32_t n = 0; ok && !mbar_try_wait_sleep(&bars.taken, phase, 1000); ++n)
-          ok = *const_cast<volatile uint32_t*>(&bars.failed) == 0 && n < (1u << 30);
-        if (!ok) break;
+        // Not asked again before every role has gone on to this one, which takes as
+        // long as the work before it.
+        if (!(ok = wait_for_roles(&bars.taken, phase, &bars.failed))) break;
       }
     }
     __syncwarp();
@@ -804,8 +810,8 @@ __global__ void __launch_bounds__(Roles<Q4>::kThreads, 1)
     else
       tc::fewer_registers<Ro::kMmaRegs>();
   }
-  // A wait that gave up leaves its role, and every role behind it gives up in
-  // its turn, seconds after the last copy or product has landed.
+  // A wait that gave up leaves its role and says so, and every role behind it gives up
+  // in its turn, seconds after the last copy or product has landed.
   if (!ok) {
     *const_cast<volatile uint32_t*>(&bars.failed) = 1;
     g_prefill_status = 1;

@@ -1,0 +1,53 @@
+"""Attention of many tokens on grids with more places than multiprocessors, where a CTA goes
+on with the work of places that have not started: barriers' phases, ring stages and tensor
+memory are carried from one place to the next."""
+import pytest
+import torch
+
+import sparse_kv_prefetch_gb300 as dd
+from paged_util import Cache, check_attention
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def test_a_place_of_seconds_beside_short_ones():
+    """Eight places of 200 million positions (one page, repeated) and 312 short ones.  The second
+    row tile of every place is empty, so its warps wait for the work of the others, longer than
+    any wait for a tile may last.
+
+    The long sequence's queries are 0 and its values powers of two.  The weights are added up by
+    tiles of 64, exact below 2^30, so lse is the logarithm of the number of positions, to the
+    rounding of the last tile and of a number above 16 (2^-19 a step).  max_kv_len = 0 keeps the
+    sums of 200 million values in one accumulator each.  Sums of up to 2^24 equal values are
+    exact in fp32 however it adds them; beyond, terms may be lost (a tensor core cuts each term
+    to its sum's last bits) but none is added twice, so a result lies between 2^24 / n of its
+    value and the value, to the rounding to bf16."""
+    heads, d, page, m, n_long = 8, 64, 128, 40, 200_000_011
+    lens = [41 + 17 * b for b in range(39)]
+    c = Cache([m] * 39, lens, heads, heads, d, page, BF, True, extra=1)
+    spare = min(set(range(c.n_pages)) - set(c.table.flatten().tolist()))
+    values = torch.tensor([(-1) ** h * 2.0 ** -h for h in range(heads)])
+    pair = torch.zeros(heads, page, d // 32, 2)
+    pair[..., 1] = values[:, None, None]
+    for i in range(2):
+        c.pools[i][spare] = 0
+        c.pools[i][spare, :, page * d // 2:] = pair.bfloat16().flatten(1).view(torch.uint8).cuda()
+    max_pages = -(-n_long // page)
+    table = torch.full((40, max_pages), -1, dtype=torch.int32, device="cuda")
+    table[0] = spare
+    table[1:, :c.max_pages] = c.table.cuda()
+    shape = dd.PagedShape(40, heads, heads, d, page, c.n_pages, max_pages, dd.DD_BF16,
+                          dd.DD_PAGES_Q4)
+    seqs = dd.PagedSeqs(torch.arange(0, 40 * m + 1, m, dtype=torch.int32).cuda(),
+                        torch.tensor([n_long] + lens, dtype=torch.int32).cuda(), table, *c.pools)
+    q = torch.cat([torch.zeros_like(c.q[:m]), c.q])
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    assert dd.paged_attn_workspace_size(shape, 40 * m, m, 0) == 0  # not split
+    dd.paged_attn(shape, seqs, q, out, lse, None, max_q_len=m, max_kv_len=0)
+    dd.check_device()
+    part = out[:m].cpu().double() / values.double()[None, :, None]
+    assert (part >= 2.0 ** 24 / n_long * (1 - 2.0 ** -8)).all() and (part <= 1 + 2.0 ** -8).all()
+    want = torch.arange(n_long - m + 1, n_long + 1, dtype=torch.double).log()
+    assert ((lse[:m].cpu().double() - want[:, None]).abs() <= 2.0 ** -19 + 2.0 ** -22).all()
+    check_attention(c, out[m:], lse[m:])
