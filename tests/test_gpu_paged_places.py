@@ -51,3 +51,74 @@ def test_a_place_of_seconds_beside_short_ones():
     want = torch.arange(n_long - m + 1, n_long + 1, dtype=torch.double).log()
     assert ((lse[:m].cpu().double() - want[:, None]).abs() <= 2.0 ** -19 + 2.0 ** -22).all()
     check_attention(c, out[m:], lse[m:])
+
+
+FORMS = [
+    # heads, kv heads, d, page, q4
+    (16, 8, 64, 32, False),
+    (8, 8, 128, 16, False),
+    (16, 8, 256, 64, False),
+    (8, 8, 64, 128, True),
+    (16, 8, 128, 64, True),
+    (8, 8, 256, 16, True),
+]
+
+
+def mixed(n, seed):
+    """n sequences of 0, 1, 33, 150 and 300 tokens, after odd numbers of others."""
+    g = torch.Generator().manual_seed(seed)
+    q_lens = [(0, 1, 33, 150, 300)[(b * 7 + seed) % 5] for b in range(n)]
+    extra = (2 * torch.randint(0, 300, (n,), generator=g) + 1).tolist()
+    return q_lens, [m + (0 if b % 4 == 0 else x) for b, (m, x) in enumerate(zip(q_lens, extra))]
+
+
+def call(c, max_q, max_kv, window=0, sinks=0):
+    """(out, lse, bytes of workspace); twice, the second time over the first one's results."""
+    n = dd.paged_attn_workspace_size(c.shape, c.n_tokens, max_q, max_kv)
+    ws = torch.empty(max(16, n), dtype=torch.uint8, device="cuda").fill_(255)
+    out, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda")
+    seqs = c.seqs()
+    first = None
+    for _ in range(2):
+        out.fill_(float("nan")), lse.fill_(float("nan"))
+        dd.paged_attn(c.shape, seqs, c.q, out, lse, ws, max_q_len=max_q, max_kv_len=max_kv,
+                      window=window, sinks=sinks)
+        if first is None:
+            first = out.clone()
+    dd.check_device()
+    assert torch.equal(out, first)
+    return out, lse, n
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 0), (130, 70)])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(map(str, f)))
+def test_mixed_sequences_on_more_places_than_multiprocessors(form, window, sinks):
+    heads, kv_heads, d, page, q4 = form
+    q_lens, kv_lens = mixed(45, d + window)
+    c = Cache(q_lens, kv_lens, heads, kv_heads, d, page, BF, q4, seed=d + sinks)
+    c.poison(window, sinks)
+    out, lse, _ = call(c, 300, max(kv_lens), window, sinks)
+    check_attention(c, out, lse, window, sinks)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(map(str, f)))
+def test_split_prompts_on_more_places_than_multiprocessors(form):
+    heads, kv_heads, d, page, q4 = form
+    c = Cache([290, 300, 0, 300, 1, 300, 300, 33, 300, 300],
+              [6001, 300, 0, 4999, 3001, 305, 700, 33, 911, 8999], heads, kv_heads, d, page, BF, q4)
+    c.poison()
+    out, lse, ws = call(c, 300, 20000)  # a hint at which every form is split
+    assert ws > 2 * c.n_tokens * heads * d * 4  # at least two splits
+    check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(map(str, f)))
+def test_sequences_of_several_turns_of_the_grid(form):
+    """More row tiles than the grid has places for: max_q_len is below the sequences' length."""
+    heads, kv_heads, d, page, q4 = form
+    lens = [300, 700, 1, 517, 0, 650] * 4
+    c = Cache(lens, [n + 61 * (b % 3) for b, n in enumerate(lens)], heads, kv_heads, d, page, BF,
+              q4)
+    c.poison(250, 3)
+    out, lse, _ = call(c, 40, 900, 250, 3)
+    check_attention(c, out, lse, 250, 3)
