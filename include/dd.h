@@ -513,7 +513,10 @@ dd_status dd_paged_read(const dd_paged_shape* shape, const dd_paged_seqs* seqs, 
  * max_q_len (at least 1) and max_kv_len (at least 0) say what the longest
  * q_start[b+1] - q_start[b] and seq_len[b] are expected to be; they choose the
  * kernel and how far a long context is split, not the result's meaning, and a
- * sequence beyond them is still computed whole.  The workspace takes
+ * sequence beyond them is still computed whole.  Sums over a context of millions of
+ * keys need its true max_kv_len: it keeps the number of terms that one fp32 sum takes
+ * at 2^18 (fp32: 2^15), beyond which the tensor cores' cutting of terms shows (some
+ * 2^-27.5 of a sum for each further one).  The workspace takes
  * dd_paged_attn_workspace_size for the same values (it may be 0 bytes, then
  * workspace may be NULL); nothing in it has to be set or kept, and calls that
  * may run at the same time need one each.  Sums and the softmax are fp32; with

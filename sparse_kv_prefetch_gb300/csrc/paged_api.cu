@@ -95,8 +95,17 @@ Plan attn_plan(const Dims& d, int max_q, int max_kv, int window, int sinks) {
       ns += 5500 + (double)n * d.B * max_q * d.Hq * d.d * 8 / 5000;
     return ns;
   };
+  // How many keys one split takes at most, whatever that costs.  A tensor core adds
+  // each term to a sum with what the sum's last place (and two bits more) leaves of it,
+  // cut, so an accumulator loses some 2^-27.5 of itself a key: 0.08 % measured after
+  // 2^17 keys of equal weights, 0.6 % after 2^20, 2.5 % after 2^22.  2^18 for the prompt
+  // kernel's one accumulator, 2^20 for the four warps' of the other; fp32 adds round
+  // instead, and 2^17 keys are 2^11 of them for a warp, 2e-5 measured.
+  const long long longest = !decode ? 1 << 18 : d.dtype == DD_F32 ? 1 << 17 : 1 << 20;
   // Tried: every number up to 16, then each some 1/8 above the last.
   auto split = [&](long long keys, int most) {
+    const int need = (int)((keys + longest - 1) / longest);
+    if (need > kMaxSplits) return need;
     const int top = (int)std::max(1ll, std::min((long long)most, (keys + least - 1) / least));
     int tried[64], k = 0;
     double ns[64], best = 0;
@@ -107,9 +116,9 @@ Plan attn_plan(const Dims& d, int max_q, int max_kv, int window, int sinks) {
     }
     while (ns[--k] > 1.04 * best) {
     }
-    return tried[k];
+    return std::max(tried[k], need);
   };
-  p.nsplit = split(max_kv, kMaxSplits);
+  p.nsplit = split(std::min(max_kv, 1 << 30), kMaxSplits);  // positions end there
   // A window leaves fewer keys; never more splits, for the workspace's sake.
   if (window > 0)
     p.nsplit = split(std::min((long long)max_kv, (long long)window + max_q + sinks), p.nsplit);
