@@ -135,13 +135,15 @@ class PagedShape:
     format: int = DD_PAGES_PLAIN
 
     def c(self) -> dd_paged_shape:
-        return _paged_shape_c(self)
+        return dd_paged_shape(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim,
+                              self.page_size, self.n_pages, self.max_pages, self.dtype,
+                              self.format)
 
 
 @functools.lru_cache(maxsize=256)
-def _paged_shape_c(s: PagedShape) -> dd_paged_shape:
-    return dd_paged_shape(s.batch, s.n_q_heads, s.n_kv_heads, s.head_dim, s.page_size, s.n_pages,
-                          s.max_pages, s.dtype, s.format)
+def _paged_ref(s: PagedShape):
+    """The structure of a shape as an argument: made once, and never handed out."""
+    return ctypes.byref(s.c())
 
 
 _L = None
@@ -494,7 +496,7 @@ class PagedSeqs:
 def paged_pool_bytes(shape: PagedShape) -> int:
     """Bytes of one pool (K or V) of a paged cache."""
     n = ctypes.c_size_t()
-    _check(_lib().dd_paged_pool_bytes(ctypes.byref(shape.c()), ctypes.byref(n)),
+    _check(_lib().dd_paged_pool_bytes(_paged_ref(shape), ctypes.byref(n)),
            "dd_paged_pool_bytes")
     return n.value
 
@@ -552,7 +554,7 @@ def paged_append(shape: PagedShape, seqs: PagedSeqs, q, k, v, q_out, rope=None,
         if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[1] != 2:
             raise ValueError("rope: expected fp32 [positions][2][rot_dim / 2]")
         rp, rl, rd = _dev(rope), rope.shape[0], 2 * rope.shape[2]
-    _check(_lib().dd_paged_append(ctypes.byref(shape.c()), ctypes.byref(seqs.c), n, qp, kp, vp,
+    _check(_lib().dd_paged_append(_paged_ref(shape), ctypes.byref(seqs.c), n, qp, kp, vp,
                                   qs or 0, ks, vs, qo, rp, rl, rd, int(interleaved),
                                   _stream(stream)), "dd_paged_append")
 
@@ -564,7 +566,7 @@ def paged_read(shape: PagedShape, seqs: PagedSeqs, first: int, count: int, k_out
     seqs.check(shape)
     need = (shape.batch * shape.n_kv_heads * count * shape.head_dim
             * (2 if shape.dtype == DD_BF16 else 4))
-    _check(_lib().dd_paged_read(ctypes.byref(shape.c()), ctypes.byref(seqs.c), first, count,
+    _check(_lib().dd_paged_read(_paged_ref(shape), ctypes.byref(seqs.c), first, count,
                                 _out(k_out, shape.dtype, need, "k_out"),
                                 _out(v_out, shape.dtype, need, "v_out"), _stream(stream)),
            "dd_paged_read")
@@ -574,7 +576,7 @@ def paged_attn_workspace_size(shape: PagedShape, n_tokens: int, max_q_len: int,
                               max_kv_len: int) -> int:
     """Bytes of workspace that paged_attn takes for these values (may be 0)."""
     n = ctypes.c_size_t()
-    _check(_lib().dd_paged_attn_workspace_size(ctypes.byref(shape.c()), n_tokens, max_q_len,
+    _check(_lib().dd_paged_attn_workspace_size(_paged_ref(shape), n_tokens, max_q_len,
                                                max_kv_len, ctypes.byref(n)),
            "dd_paged_attn_workspace_size")
     return n.value
@@ -592,7 +594,7 @@ def paged_attn(shape: PagedShape, seqs: PagedSeqs, q, out, lse_out=None, workspa
         raise ValueError("out: expected a contiguous tensor")
     lp = None if lse_out is None else _out(lse_out, DD_F32, 4 * n * shape.n_q_heads, "lse_out")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib().dd_paged_attn(ctypes.byref(shape.c()), ctypes.byref(seqs.c), n, qp, qs,
+    _check(_lib().dd_paged_attn(_paged_ref(shape), ctypes.byref(seqs.c), n, qp, qs,
                                 max_q_len, max_kv_len, window, sinks, op, lp, _dev(workspace),
                                 ws_bytes, _stream(stream)), "dd_paged_attn")
 

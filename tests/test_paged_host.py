@@ -1,0 +1,21 @@
+"""The paged cache's binding and limits, on the host (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import sparse_kv_prefetch_gb300 as dd
+
+
+def _shape(**kw):
+    base = dict(batch=2, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=16, n_pages=10,
+                max_pages=4, dtype=dd.DD_BF16, format=dd.DD_PAGES_PLAIN)
+    base.update(kw)
+    return dd.PagedShape(**base)
+
+
+def test_a_shape_hands_out_structures_of_its_own():
+    """Writing to the structure of one shape changes no other call of an equal shape."""
+    want = dd.paged_pool_bytes(_shape())
+    c = _shape().c()
+    c.n_pages = 1000
+    assert _shape().c().n_pages == 10 and dd.paged_pool_bytes(_shape()) == want
