@@ -142,19 +142,26 @@ dd_status resolve_landmarks(const dd_shape* s, int chunk, LandmarkDims* out) {
   return DD_OK;
 }
 
-// Device memory of the current device, or managed memory.
-static bool is_device_ptr_on(const void* p, int dev) {
+// Device memory of the current device (*dev, asked for once if it is -1), or managed memory.
+// A failed query leaves no error behind for a later call to report.
+static bool is_device_ptr_on(const void* p, int* dev) {
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == dev);
+  if (a.type == cudaMemoryTypeManaged) return true;
+  if (a.type != cudaMemoryTypeDevice) return false;
+  if (*dev < 0 && cudaGetDevice(dev) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return a.device == *dev;
 }
 
 bool is_device_ptr(const void* p) {
   int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess && is_device_ptr_on(p, dev);
+  return is_device_ptr_on(p, &dev);
 }
 
 bool lsu_gather_fits(const Dims& d) {
@@ -163,9 +170,8 @@ bool lsu_gather_fits(const Dims& d) {
 
 bool all_device(std::initializer_list<const void*> ps) {
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
   for (const void* p : ps)
-    if (p && !is_device_ptr_on(p, dev)) return false;
+    if (p && !is_device_ptr_on(p, &dev)) return false;
   return true;
 }
 

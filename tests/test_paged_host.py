@@ -19,3 +19,16 @@ def test_a_shape_hands_out_structures_of_its_own():
     c = _shape().c()
     c.n_pages = 1000
     assert _shape().c().n_pages == 10 and dd.paged_pool_bytes(_shape()) == want
+
+
+def test_pointer_checks_ask_for_a_device_only_when_a_pointer_needs_one():
+    """Absent pointers are no host pointers, with a device or without."""
+    f = getattr(dd.lib(), "_ZN2dd10all_deviceESt16initializer_listIPKvE")
+    f.argtypes, f.restype = [ctypes.c_void_p, ctypes.c_size_t], ctypes.c_bool
+    two = (ctypes.c_void_p * 2)()
+    assert f(two, 2) and f(two, 0)
+    two[1] = ctypes.addressof(two)
+    assert not f(two, 2)
+    # and a refusal leaves no error behind
+    peek = ctypes.CDLL("libcudart.so.13").cudaPeekAtLastError
+    assert peek() == 0
