@@ -29,6 +29,3 @@ def test_pointer_checks_ask_for_a_device_only_when_a_pointer_needs_one():
     assert f(two, 2) and f(two, 0)
     two[1] = ctypes.addressof(two)
     assert not f(two, 2)
-    # and a refusal leaves no error behind
-    peek = ctypes.CDLL("libcudart.so.13").cudaPeekAtLastError
-    assert peek() == 0
