@@ -823,7 +823,7 @@ cudaError_t launch_nr(const Dims& d, const Seqs& s, const AttnArgs& a, cudaStrea
   constexpr int smem = ring > merge ? ring : merge;
   cudaError_t e = prepare_kernel(decode_kernel<D, K, NR>, &prepared, smem);
   if (e != cudaSuccess) return e;
-  const long long chunks = ((long long)a.max_q * d.G + 8 * NR - 1) / (8 * NR);
+  const long long chunks = ((long long)min(a.max_q, s.n_tokens) * d.G + 8 * NR - 1) / (8 * NR);
   const dim3 grid((unsigned)(d.B * d.Hkv), (unsigned)(chunks < 65535 ? chunks : 65535),
                   (unsigned)a.nsplit);
   cudaLaunchAttribute cluster;

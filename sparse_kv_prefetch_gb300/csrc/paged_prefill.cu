@@ -875,7 +875,8 @@ cudaError_t launch(const Dims& d, const Seqs& s, const AttnArgs& a, cudaStream_t
            !make_map(&km, s.k, D, d.page, (uint64_t)d.n_pages * d.Hkv, row, row * d.page, sub, 1) ||
            !make_map(&vm, s.v, D, d.page, (uint64_t)d.n_pages * d.Hkv, row, row * d.page, sub, 1))
     return cudaErrorInvalidValue;
-  const long long tiles = ((long long)a.max_q * d.G + Ge::kRows - 1) / Ge::kRows;
+  const long long tiles =
+      ((long long)min(a.max_q, s.n_tokens) * d.G + Ge::kRows - 1) / Ge::kRows;
   const dim3 grid((unsigned)(d.B * d.Hkv), (unsigned)(tiles < 65535 ? tiles : 65535),
                   (unsigned)a.nsplit);
   prefill_kernel<D, NT, BN, Q4><<<grid, Roles<Q4>::kThreads, Ge::kSmem, st>>>(
