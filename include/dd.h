@@ -432,7 +432,8 @@ dd_status dd_score_topk_landmarks(const dd_shape* shape, int chunk, const void* 
  * A call without tokens (n_tokens = 0) or positions (count = 0) returns DD_OK
  * and launches nothing.  Supported: head_dim and H_q / H_kv as above; page_size 16, 32, 64 or 128;
  * max_pages * page_size and n_pages * H_kv * page_size at most 2^30; B * H_kv
- * at most 2^24.
+ * at most 2^24.  A call beyond the largest grid (2^31 - 1 CTAs, hundreds of GB of
+ * outputs) returns DD_ERR_UNSUPPORTED.
  */
 typedef enum { DD_PAGES_PLAIN = 0, DD_PAGES_Q4 = 1 } dd_page_format;
 

@@ -39,6 +39,10 @@ struct AppendArgs {
   const float* rope;
   int rope_len, rot_dim, interleaved;
 };
+// CTAs that a call takes; the launches need kMaxBlocks at most.
+constexpr long long kMaxBlocks = 0x7FFFFFFF;
+long long append_blocks(const Dims& d, int n_tokens, bool with_q);
+long long read_blocks(const Dims& d, int count);
 cudaError_t launch_append(const Dims& d, const Seqs& s, const AppendArgs& a, cudaStream_t st);
 
 cudaError_t launch_read(const Dims& d, const Seqs& s, int first, int count, void* k_out,

@@ -210,6 +210,8 @@ dd_status dd_paged_append(const dd_paged_shape* shape, const dd_paged_seqs* seqs
       !stride_ok(v_stride, d.Hkv, d))
     return DD_ERR_INVALID_ARG;
   if (q && q == q_out && q_stride != (int64_t)d.Hq * d.d) return DD_ERR_INVALID_ARG;
+  if (paged::append_blocks(d, n_tokens, q != nullptr) > paged::kMaxBlocks)
+    return DD_ERR_UNSUPPORTED;
   Seqs s;
   st = resolve_seqs(d, seqs, n_tokens, true, &s);
   if (st != DD_OK) return st;
@@ -227,6 +229,7 @@ dd_status dd_paged_read(const dd_paged_shape* shape, const dd_paged_seqs* seqs, 
   if (first < 0 || count < 0 || first > kMaxTokens || count > kMaxTokens) return DD_ERR_INVALID_ARG;
   if (count == 0) return DD_OK;
   if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return DD_ERR_INVALID_ARG;
+  if (paged::read_blocks(d, count) > paged::kMaxBlocks) return DD_ERR_UNSUPPORTED;
   Seqs s;
   st = resolve_seqs(d, seqs, 0, false, &s);
   if (st != DD_OK) return st;
@@ -265,6 +268,7 @@ dd_status dd_paged_attn(const dd_paged_shape* shape, const dd_paged_seqs* seqs, 
   window = std::min(window, 1 << 30);
   sinks = std::min(sinks, 1 << 30);
   const paged::Plan p = paged::attn_plan(d, max_q_len, max_kv_len, window, sinks);
+  if (p.merged && (long long)n_tokens * d.Hq > paged::kMaxBlocks) return DD_ERR_UNSUPPORTED;
   const AttnWs w = attn_ws(d, n_tokens, p);
   if (w.total > 0 && (!workspace || ws_bytes < w.total)) return DD_ERR_INVALID_ARG;
   Seqs s;

@@ -300,24 +300,36 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
+// Warps for a token's queries and for its keys (as many for its values): heads by
+// the lanes that share one.
+struct Warps {
+  int q, k;
+};
+Warps warps_of(const Dims& d, bool with_q) {
+  const int pieces = d.d * d.elt / 16;
+  const int hq = kHeads * (32 / (pieces / 2));
+  const int hk = d.format == DD_PAGES_Q4 ? kHeads * (32 / pieces) : hq;
+  return Warps{with_q ? (d.Hq + hq - 1) / hq : 0, (d.Hkv + hk - 1) / hk};
+}
+
 template <typename T, int D, bool Q4>
 cudaError_t launch(const Dims& d, const Seqs& s, const AppendArgs& a, cudaStream_t st) {
   static unsigned long long prepared = 0;
   cudaError_t e = prepare_kernel(append_kernel<T, D, Q4>, &prepared, 0);
   if (e != cudaSuccess) return e;
-  // Heads that a warp takes, by the lanes that share one.
-  const int hq = kHeads * (32 / Geo<T, D>::kUnits);
-  const int hk = Q4 ? kHeads * (32 / Geo<T, D>::kPieces) : hq;
-  const int wq = a.q ? (d.Hq + hq - 1) / hq : 0;
-  const int wk = (d.Hkv + hk - 1) / hk;
-  const long long blocks = ((long long)s.n_tokens * (wq + 2 * wk) + kWarps - 1) / kWarps;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  const Warps w = warps_of(d, a.q != nullptr);
   append_kernel<T, D, Q4>
-      <<<(unsigned)blocks, kWarps * 32, 0, st>>>(s, a, d.Hq, d.Hkv, wq, wk);
+      <<<(unsigned)append_blocks(d, s.n_tokens, a.q != nullptr), kWarps * 32, 0, st>>>(
+          s, a, d.Hq, d.Hkv, w.q, w.k);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+long long append_blocks(const Dims& d, int n_tokens, bool with_q) {
+  const Warps w = warps_of(d, with_q);
+  return ((long long)n_tokens * (w.q + 2 * w.k) + kWarps - 1) / kWarps;
+}
 
 cudaError_t launch_append(const Dims& d, const Seqs& s, const AppendArgs& a, cudaStream_t st) {
   if (d.format == DD_PAGES_Q4) {

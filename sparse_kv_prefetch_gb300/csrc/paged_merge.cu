@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(128)
 
 cudaError_t launch_attn_merge(const Dims& d, const Seqs& s, const AttnArgs& a, cudaStream_t st) {
   const long long rows = (long long)s.n_tokens * d.Hq;
-  if (rows > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   const unsigned g = (unsigned)rows;
   if (d.dtype == DD_BF16) {
     if (d.d == 64) attn_merge_kernel<bf16_t, 64><<<g, 128, 0, st>>>(s, a, d.Hq, rows);

@@ -74,22 +74,29 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// CTAs of one (sequence, KV head).
+int tiles_of(const Dims& d, int count) {
+  const long long n = (long long)count * (d.d * d.elt / 16);
+  return (int)((n + kThreads * kPer - 1) / (kThreads * kPer));
+}
+
 template <typename T, int D, bool Q4>
 cudaError_t launch(const Dims& d, const Seqs& s, int first, int count, void* k_out, void* v_out,
                    cudaStream_t st) {
   static unsigned long long prepared = 0;
   cudaError_t e = prepare_kernel(read_kernel<T, D, Q4>, &prepared, 0);
   if (e != cudaSuccess) return e;
-  const long long n = (long long)count * (D / Elem<T>::kVec);
-  const long long tiles = (n + kThreads * kPer - 1) / (kThreads * kPer);
-  const long long blocks = tiles * d.B * d.Hkv;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  read_kernel<T, D, Q4><<<(unsigned)blocks, kThreads, 0, st>>>(
-      s, d.Hkv, first, count, (int)tiles, static_cast<uint4*>(k_out), static_cast<uint4*>(v_out));
+  read_kernel<T, D, Q4><<<(unsigned)read_blocks(d, count), kThreads, 0, st>>>(
+      s, d.Hkv, first, count, tiles_of(d, count), static_cast<uint4*>(k_out),
+      static_cast<uint4*>(v_out));
   return cudaGetLastError();
 }
 
 }  // namespace
+
+long long read_blocks(const Dims& d, int count) {
+  return (long long)tiles_of(d, count) * d.B * d.Hkv;
+}
 
 cudaError_t launch_read(const Dims& d, const Seqs& s, int first, int count, void* k_out,
                         void* v_out, cudaStream_t st) {

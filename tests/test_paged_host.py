@@ -29,3 +29,26 @@ def test_pointer_checks_ask_for_a_device_only_when_a_pointer_needs_one():
     assert f(two, 2) and f(two, 0)
     two[1] = ctypes.addressof(two)
     assert not f(two, 2)
+
+
+def test_calls_beyond_the_largest_grid_are_unsupported():
+    """Refused by their sizes, before anything is launched."""
+    L, most = dd.lib(), 1 << 30
+    s = _shape(n_q_heads=64, n_kv_heads=64, head_dim=64, batch=64)
+    seqs = dd.dd_paged_seqs(16, 16, 16, 16, 16)
+
+    def append(n, q):
+        return L.dd_paged_append(ctypes.byref(s.c()), ctypes.byref(seqs), n, q, 16, 16, 64 * 64,
+                                 64 * 64, 64 * 64, q and 32, None, 0, 0, 0, None)
+
+    def read(count):
+        return L.dd_paged_read(ctypes.byref(s.c()), ctypes.byref(seqs), 0, count, 16, 16, None)
+
+    def attn(n):  # split: merged by a grid of a CTA for every row
+        return L.dd_paged_attn(ctypes.byref(s.c()), ctypes.byref(seqs), n, 16, 64 * 64, 1, most, 0,
+                               0, 16, None, 16, 1 << 62, None)
+
+    # within the grid the addresses are what is refused
+    assert append(most, 16) == dd.DD_ERR_UNSUPPORTED and append(1000, 16) == dd.DD_ERR_INVALID_ARG
+    assert read(most) == dd.DD_ERR_UNSUPPORTED and read(1000) == dd.DD_ERR_INVALID_ARG
+    assert attn(most) == dd.DD_ERR_UNSUPPORTED and attn(1000) == dd.DD_ERR_INVALID_ARG
