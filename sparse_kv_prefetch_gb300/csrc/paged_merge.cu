@@ -68,20 +68,28 @@ __global__ void __launch_bounds__(128)
   if (a.lse && threadIdx.x == 0) a.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
+template <typename T, int D>
+cudaError_t launch(const Dims& d, const Seqs& s, const AttnArgs& a, cudaStream_t st) {
+  static unsigned long long prepared = 0;
+  cudaError_t e = prepare_kernel(attn_merge_kernel<T, D>, &prepared, 0);
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)s.n_tokens * d.Hq;
+  attn_merge_kernel<T, D><<<(unsigned)rows, 128, 0, st>>>(s, a, d.Hq, rows);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_attn_merge(const Dims& d, const Seqs& s, const AttnArgs& a, cudaStream_t st) {
-  const long long rows = (long long)s.n_tokens * d.Hq;
-  const unsigned g = (unsigned)rows;
   if (d.dtype == DD_BF16) {
-    if (d.d == 64) attn_merge_kernel<bf16_t, 64><<<g, 128, 0, st>>>(s, a, d.Hq, rows);
-    if (d.d == 128) attn_merge_kernel<bf16_t, 128><<<g, 128, 0, st>>>(s, a, d.Hq, rows);
-    if (d.d == 256) attn_merge_kernel<bf16_t, 256><<<g, 128, 0, st>>>(s, a, d.Hq, rows);
+    if (d.d == 64) return launch<bf16_t, 64>(d, s, a, st);
+    if (d.d == 128) return launch<bf16_t, 128>(d, s, a, st);
+    if (d.d == 256) return launch<bf16_t, 256>(d, s, a, st);
   } else {
-    if (d.d == 64) attn_merge_kernel<float, 64><<<g, 128, 0, st>>>(s, a, d.Hq, rows);
-    if (d.d == 128) attn_merge_kernel<float, 128><<<g, 128, 0, st>>>(s, a, d.Hq, rows);
+    if (d.d == 64) return launch<float, 64>(d, s, a, st);
+    if (d.d == 128) return launch<float, 128>(d, s, a, st);
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace paged

@@ -24,3 +24,75 @@ def test_a_length_hint_beyond_the_call_costs_nothing(dtype, q4):
     b.synchronize()
     assert a.elapsed_time(b) < 20
     dd.check_device()
+
+
+def captured_split_call(heads, kv_heads, d, page, dtype, q4, tokens, most):
+    """A call that is split and merged through the workspace, captured as the first of its kind
+    and replayed over other lengths, tables and pools, the workspace full of NaN each time."""
+    lens = [([tokens, tokens], [most, tokens + 1]), ([1, 2 * tokens - 1], [17, most - 40]),
+            ([2 * tokens, 0], [most - 3, 9])]
+    if tokens == 1:
+        lens = [([1, 1], [most, 2]), ([1, 1], [17, most - 40]), ([0, 1], [9, most - 3])]
+    caches = [Cache(q, n, heads, kv_heads, d, page, dtype, q4, seed=i, behind=2 * tokens - sum(q),
+                    extra=2 * -(-most // page) - sum(-(-x // page) for x in n))
+              for i, (q, n) in enumerate(lens)]
+    rows = max(c.max_pages for c in caches)
+    T, n_pages = 2 * tokens, caches[0].n_pages
+    shape = dd.PagedShape(2, heads, kv_heads, d, page, n_pages, rows, caches[0].shape.dtype,
+                          caches[0].shape.format)
+    pools = [torch.zeros_like(p) for p in caches[0].pools]
+    q_start, seq_len = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (3, 2))
+    table = torch.full((2, rows), -1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(T, heads, d, dtype=dtype, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(T, heads, device="cuda")
+    seqs = dd.PagedSeqs(q_start, seq_len, table, *pools)
+    size = dd.paged_attn_workspace_size(shape, T, T if tokens > 1 else 1, 40000)
+    splits = size // (T * heads * (4 * d + 8))
+    assert splits > 8 if tokens == 1 else splits > 1
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dd.paged_attn(shape, seqs, q, out, lse, ws, max_q_len=T if tokens > 1 else 1,
+                      max_kv_len=40000)
+    for c in caches:
+        assert c.n_pages == n_pages
+        c.poison()
+        for p, x in zip(pools, c.pools):
+            p.copy_(x)
+        q_start.copy_(torch.tensor(c.q_start, dtype=torch.int32))
+        seq_len.copy_(torch.tensor(c.kv_lens, dtype=torch.int32))
+        table.fill_(-1)
+        table[:, :c.max_pages] = c.table.cuda()
+        q.copy_(c.q)
+        ws.fill_(255)
+        out.fill_(3.0)
+        graph.replay()
+        check_attention(c, out, lse)
+        assert (out[c.q_start[2]:] == 3).all()  # rows of no sequence
+    dd.check_device()
+
+
+MERGED = [(8, 2, 128, 64, BF, False), (4, 4, 64, 16, F32, False), (8, 1, 256, 32, BF, False),
+          (2, 2, 64, 16, BF, True)]
+
+
+# (fp32 calls of many rows are split into clusters, which need no workspace)
+@pytest.mark.parametrize("form,tokens", [(f, t) for f in MERGED for t in (1, 40)
+                                         if t == 1 or f[4] == BF])
+def test_captured_split_calls(form, tokens):
+    captured_split_call(*form, tokens, 9000)
+
+
+def test_the_first_call_of_a_process_may_be_a_captured_split_one():
+    """In a process of its own, where no kernel has been used before the capture."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import torch, test_gpu_paged_calls as t\n"
+            "t.captured_split_call(8, 2, 128, 64, torch.bfloat16, False, 1, 9000)\n"
+            "t.captured_split_call(8, 2, 128, 64, torch.bfloat16, True, 40, 3000)\n"
+            % (os.path.dirname(here), here))
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
