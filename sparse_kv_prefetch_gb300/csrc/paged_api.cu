@@ -58,7 +58,8 @@ Plan attn_plan(const Dims& d, int max_q, int max_kv, int window, int sinks) {
   // tcgen05, over 4000 keys 31 against 42; with 12 tokens 387 and 369; bf16 188
   // and 179), and fp32 always: its products do not run on tcgen05.  (On the CUDA
   // cores, 64 rows to a CTA, 2048 and 700 tokens took 1402 us with d = 128 and 691
-  // with d = 64, where this takes 1403 and 498; 980 tokens of 4 heads 260 and 122.)
+  // with d = 64, where this takes 1450 and 503; 980 tokens of 4 heads 260 and 122,
+  // here 68 and 31.)
   const bool q4 = d.format == DD_PAGES_Q4;
   p.path = d.dtype == DD_F32 || rows <= (q4 ? 32 : 16) ? kDecode : kPrefill;
   // How far the keys are split, by an estimate in ns from measured rates (bytes

@@ -43,7 +43,8 @@
 // and a product is hi hi + hi lo + lo hi: 2^-21 relative, of the order of the
 // fp32 sums' own rounding.  P goes to the second product over shuffles.  fp32
 // calls of many tokens run here too, 16 rows at a time: 2048 and 700 tokens (32 /
-// 8 heads, d = 128) 1.40 ms, 27 TFLOP/s, bound by the splitting's instructions.
+// 8 heads, d = 128) 1.45 ms, 26 TFLOP/s, bound by the splitting's instructions.
+// Infinities do not split: rows that meet one are computed again in plain fp32.
 #include <math.h>
 
 #include "paged.cuh"
@@ -269,6 +270,62 @@ __device__ __forceinline__ uint32_t piece_at(int r, int p) {
   constexpr int kRowsPerLine = G::kRow >= 128 ? 1 : 128 / G::kRow;
   constexpr int kMask = (G::kPieces < 8 ? G::kPieces : 8) - 1;
   return r * G::kRow + 16 * (p ^ ((r / kRowsPerLine) & kMask));
+}
+
+// A warp's part of fp32 rows again, for sums that the split products left without a
+// finite value: an infinity has no finite rest (and the largest fp32 round to one in
+// tf32), so there it becomes NaN.  A key and a row at a time; rows of D + 4 into po,
+// (max, sum) into pml.  Where the warp's keys lie is found again, so that the kernel
+// keeps no registers for it; as a function of its own it costs calls of many rows of
+// 512 bytes 3 % (1404 us without, 1450 with, 1506 inlined), others nothing.
+template <int D>
+__device__ __noinline__ void in_plain_fp32(Seqs s, AttnArgs a, int Hkv, int G, int warps,
+                                           long long r0, int nr, float k1, float* po,
+                                           float2* pml) {
+  constexpr int E = D / 32;  // elements of a lane
+  const int b = blockIdx.x / Hkv, hk = blockIdx.x - b * Hkv, split = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, page = 1 << s.log2_page;
+  const Seq q = load_seq(s, b);
+  const KeyTiles kt = key_tiles<16>(q.pos0 + (int)(r0 / G), q.pos0 + (int)((r0 + nr - 1) / G),
+                                    q.len, a.window, a.sinks);
+  const int i0 = (int)((long long)kt.n * split / a.nsplit);
+  const int i1 = (int)((long long)kt.n * (split + 1) / a.nsplit);
+#pragma unroll 1
+  for (int r = 0; r < nr; ++r) {
+    const int token = (int)((r0 + r) / G), p = q.pos0 + token;
+    const float* qr =
+        reinterpret_cast<const float*>(static_cast<const unsigned char*>(a.q) +
+                                       (size_t)(q.q0 + token) * a.q_stride) +
+        (hk * G + (int)((r0 + r) % G)) * D + E * lane;
+    float acc[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int x = 16 * (i0 + warp); x < 16 * i1; x += (x & 15) < 15 ? 1 : 16 * warps - 15) {
+      const int j = kt.tile(x >> 4) * 16 + (x & 15);
+      const int pg = page_of(s, b, j);
+      if (pg < 0 || !sees(p, j, a.window, a.sinks)) continue;
+      const size_t at = ((size_t)pg * Hkv + hk) * s.block_bytes +
+                        (size_t)((j & (page - 1)) * D + E * lane) * 4;
+      const float* kr = reinterpret_cast<const float*>(s.k + at);
+      const float* vr = reinterpret_cast<const float*>(s.v + at);
+      float y = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) y = fmaf(__ldg(qr + e), __ldg(kr + e), y);
+#pragma unroll
+      for (int z = 16; z > 0; z >>= 1) y += __shfl_xor_sync(0xffffffffu, y, z);
+      const float to = fmaxf(m, y);
+      const float f = to == -INFINITY ? 1.f : exp2a((m - to) * k1);
+      const float w = y == -INFINITY ? 0.f : exp2a((y - to) * k1);
+      m = to;
+      l = fmaf(l, f, w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * __ldg(vr + e));
+    }
+    if (lane == 0) pml[r] = make_float2(m, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) po[r * (D + 4) + E * lane + e] = acc[e];
+  }
 }
 
 template <int D, Kind K, int NR>
@@ -766,30 +823,40 @@ __global__ void __launch_bounds__((32 * Geo<D, K>::warps(NR)), (Geo<D, K>::ctas(
       acc.z = fmaf(f, x.z, acc.z);
       acc.w = fmaf(f, x.w, acc.w);
     };
-    for (int y = threadIdx.x; y < nr * (D / 4); y += kThreads) {
-      const int r = y / (D / 4), d = 4 * (y % (D / 4));
-      float M = -INFINITY;
+#pragma unroll 1
+    for (bool last = K != kF32;; last = true) {
+      float worst = 0.f;  // NaN if a sum is not finite
+      for (int y = threadIdx.x; y < nr * (D / 4); y += kThreads) {
+        const int r = y / (D / 4), d = 4 * (y % (D / 4));
+        float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, pml[w * 8 * NR + r].x);
-      const float base = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, pml[w * 8 * NR + r].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        add(pml[w * 8 * NR + r],
-            *reinterpret_cast<const float4*>(po + (w * 8 * NR + r) * LD + d), base, L, v);
-      if (a.nsplit == 1) {
-        finish(r, d, M, L, v);
-      } else if (a.part_o) {
-        const long long rr = r0 + r;
-        const size_t row = (size_t)(q.q0 + (int)(rr / G)) * Hq + hk * G + (int)(rr % G);
-        const size_t at = (size_t)split * s.n_tokens * Hq + row;
-        *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
-        if (d == 0) a.part_ml[at] = make_float2(M * (scale * (Q4 ? 16.f : 1.f)), L);
-      } else {
-        *reinterpret_cast<float4*>(res + r * D + d) = v;
-        if (d == 0) res_ml[r] = make_float2(M, L);
+        for (int w = 0; w < kWarps; ++w)
+          add(pml[w * 8 * NR + r],
+              *reinterpret_cast<const float4*>(po + (w * 8 * NR + r) * LD + d), base, L, v);
+        if (K == kF32)
+          worst = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, fmaf(L, 0.f, worst)))));
+        if (a.nsplit == 1) {
+          finish(r, d, M, L, v);
+        } else if (a.part_o) {
+          const long long rr = r0 + r;
+          const size_t row = (size_t)(q.q0 + (int)(rr / G)) * Hq + hk * G + (int)(rr % G);
+          const size_t at = (size_t)split * s.n_tokens * Hq + row;
+          *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
+          if (d == 0) a.part_ml[at] = make_float2(M * (scale * (Q4 ? 16.f : 1.f)), L);
+        } else {
+          *reinterpret_cast<float4*>(res + r * D + d) = v;
+          if (d == 0) res_ml[r] = make_float2(M, L);
+        }
       }
+      if (last || !__syncthreads_or(worst != 0.f)) break;
+      in_plain_fp32<D>(s, a, Hkv, G, kWarps, r0, nr, k1, po + warp * 8 * NR * LD,
+                       pml + warp * 8 * NR);
+      __syncthreads();
     }
     if (a.nsplit > 1 && !a.part_o) {
       cluster_sync();  // every CTA's sums are there

@@ -96,3 +96,51 @@ def test_the_first_call_of_a_process_may_be_a_captured_split_one():
             % (os.path.dirname(here), here))
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+F32_FORMS = [(4, 4, 64, 16), (8, 1, 128, 16), (2, 2, 128, 64)]
+
+
+@pytest.mark.parametrize("tokens,most", [(1, 0), (1, 20000), (3, 0), (50, 0)])
+@pytest.mark.parametrize("form", F32_FORMS, ids=lambda f: "-".join(map(str, f)))
+def test_fp32_keys_of_logit_minus_infinity_have_no_weight(form, tokens, most):
+    """Pages whose every key has the logit -infinity for every query count as no page."""
+    heads, kv_heads, d, page = form
+    c = Cache([tokens, tokens], [900, tokens + 70], heads, kv_heads, d, page, F32)
+    c.q[..., 5] = c.q[..., 5].abs() + 0.25
+    for b, i in ((0, 3), (0, 7), (1, 0)):
+        c.pools[0][int(c.table[b, i]), :, :, 5] = -torch.inf
+    out, lse = run_attention(c, max_kv=max(most, 900))
+    for b, i in ((0, 3), (0, 7), (1, 0)):
+        c.table[b, i] = -1
+    check_attention(c, out, lse)
+    dd.check_device()
+
+
+@pytest.mark.parametrize("tokens,most", [(1, 0), (1, 20000), (3, 0), (50, 0)])
+@pytest.mark.parametrize("form", F32_FORMS, ids=lambda f: "-".join(map(str, f)))
+def test_fp32_infinite_values_stay_in_their_elements_and_rows(form, tokens, most):
+    """A token that sees an infinite value has it in that element and no other; a token that does
+    not has none; of a key with logit +infinity nothing is known but that rows before it are
+    untouched."""
+    heads, kv_heads, d, page = form
+    n, at = 900, 899 - tokens // 2
+    c = Cache([tokens, 1], [n, 33], heads, kv_heads, d, page, F32)
+    where = (int(c.table[0, at // page]), slice(None), at % page)
+    c.pools[1][where + (9,)] = torch.inf
+    out, lse = run_attention(c, max_kv=max(most, n))
+    sees = slice(at - (n - tokens), tokens)
+    assert (out[sees, :, 9] == torch.inf).all()
+    c.pools[1][where + (9,)] = 0.5
+    fixed, _ = run_attention(c)
+    out[sees, :, 9] = fixed[sees, :, 9]
+    check_attention(c, out, lse)
+    c.pools[0][where + (5,)] = torch.inf
+    out, lse = run_attention(c, max_kv=max(most, n))
+    before = torch.ones(tokens + 1, dtype=torch.bool)
+    before[sees] = False
+    assert out[before].isfinite().all() and lse[before].isfinite().all()
+    c.pools[0][where + (5,)] = 0.0
+    fixed, fixed_lse = run_attention(c)
+    out[sees], lse[sees] = fixed[sees], fixed_lse[sees]
+    check_attention(c, out, lse)
