@@ -478,11 +478,17 @@ class PagedSeqs:
         self._checked = None
         self._size = [x.numel() * x.element_size() if hasattr(x, "numel") else None
                       for x in self._keep]
+        dims = getattr(page_table, "shape", ())
+        self._row = dims[1] if len(dims) == 2 else None
 
     def check(self, shape: PagedShape):
-        """Refuse tensors with fewer bytes than the shape makes the kernels read or write."""
+        """Refuse tensors with fewer bytes than the shape makes the kernels read or write, and a
+        table whose rows are not max_pages entries apart."""
         if self._checked is shape:
             return
+        if self._row not in (None, shape.max_pages):
+            raise ValueError(f"page_table with rows of {self._row} entries; the shape says "
+                             f"{shape.max_pages}")
         pool = paged_pool_bytes(shape)
         need = (4 * (shape.batch + 1), 4 * shape.batch, 4 * shape.batch * shape.max_pages, pool,
                 pool)

@@ -144,3 +144,20 @@ def test_fp32_infinite_values_stay_in_their_elements_and_rows(form, tokens, most
     fixed, fixed_lse = run_attention(c)
     out[sees], lse[sees] = fixed[sees], fixed_lse[sees]
     check_attention(c, out, lse)
+
+
+def test_a_table_with_rows_of_another_length_is_refused():
+    """The kernels step from row to row by max_pages; a flat table has no rows to compare."""
+    c = Cache([1, 1], [40, 30])
+    wide = torch.full((2, c.max_pages + 3), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.max_pages] = c.table.cuda()
+    q_start, seq_len = (torch.tensor(x, dtype=torch.int32).cuda() for x in (c.q_start, c.kv_lens))
+    out = torch.empty_like(c.q)
+    with pytest.raises(ValueError):
+        dd.paged_attn(c.shape, dd.PagedSeqs(q_start, seq_len, wide, *c.pools), c.q, out,
+                      max_q_len=1, max_kv_len=40)
+    with pytest.raises(ValueError):
+        dd.paged_read(c.shape, dd.PagedSeqs(None, seq_len, wide, *c.pools), 0, 1, out, out)
+    flat = dd.PagedSeqs(q_start, seq_len, c.table.cuda().flatten(), *c.pools)
+    out, lse = run_attention(c, seqs=flat)
+    check_attention(c, out, lse)
