@@ -589,7 +589,8 @@ def paged_attn_workspace_size(shape: PagedShape, n_tokens: int, max_q_len: int,
 
 
 def paged_attn(shape: PagedShape, seqs: PagedSeqs, q, out, lse_out=None, workspace=None, *,
-               max_q_len: int, max_kv_len: int, window: int = 0, sinks: int = 0, stream=None):
+               max_q_len: int, max_kv_len: int, window: int = 0, sinks: int = 0, stream=None,
+               ws_bytes: Optional[int] = None):
     """Causal attention of the call's tokens over their pages, with an optional sliding window
     and sinks (the first positions, always visible); see dd.h."""
     seqs.check(shape)
@@ -599,7 +600,8 @@ def paged_attn(shape: PagedShape, seqs: PagedSeqs, q, out, lse_out=None, workspa
     if os_ != shape.n_q_heads * shape.head_dim:
         raise ValueError("out: expected a contiguous tensor")
     lp = None if lse_out is None else _out(lse_out, DD_F32, 4 * n * shape.n_q_heads, "lse_out")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib().dd_paged_attn(_paged_ref(shape), ctypes.byref(seqs.c), n, qp, qs,
                                 max_q_len, max_kv_len, window, sinks, op, lp, _dev(workspace),
                                 ws_bytes, _stream(stream)), "dd_paged_attn")

@@ -161,3 +161,34 @@ def test_a_table_with_rows_of_another_length_is_refused():
     flat = dd.PagedSeqs(q_start, seq_len, c.table.cuda().flatten(), *c.pools)
     out, lse = run_attention(c, seqs=flat)
     check_attention(c, out, lse)
+
+
+def test_a_workspace_by_its_address():
+    """Raw addresses with their size, as the other calls take them."""
+    c = Cache([1], [9000])
+    n = dd.paged_attn_workspace_size(c.shape, 1, 1, 9000)
+    assert n > 0
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(c.q), torch.empty(1, 8, device="cuda")
+    kw = dict(max_q_len=1, max_kv_len=9000)
+    dd.paged_attn(c.shape, c.seqs(), c.q, out, lse.data_ptr(), ws.data_ptr(), ws_bytes=n, **kw)
+    check_attention(c, out, lse)
+    with pytest.raises(dd.DDError):
+        dd.paged_attn(c.shape, c.seqs(), c.q, out, lse, ws.data_ptr(), ws_bytes=n - 1, **kw)
+    with pytest.raises(dd.DDError):
+        dd.paged_attn(c.shape, c.seqs(), c.q, out, lse, ws, ws_bytes=n - 1, **kw)
+
+
+@pytest.mark.parametrize("tokens,most", [(1, 0), (1, 20000), (3, 0), (50, 0), (50, 20000)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_bf16_keys_of_logit_minus_infinity_have_no_weight(d, tokens, most):
+    """Pages whose every key has the logit -infinity for every query count as no page."""
+    c = Cache([tokens, tokens], [900, tokens + 70], 8, 2, d, 32)
+    c.q[..., 5] = c.q[..., 5].abs() + 0.25
+    for b, i in ((0, 0), (0, 3), (0, 7), (1, 0)):
+        c.pools[0][int(c.table[b, i]), :, :, 5] = -torch.inf
+    out, lse = run_attention(c, max_kv=max(most, 900))
+    for b, i in ((0, 0), (0, 3), (0, 7), (1, 0)):
+        c.table[b, i] = -1
+    check_attention(c, out, lse)
+    dd.check_device()
