@@ -58,7 +58,7 @@ struct AttnArgs {
   float* lse;  // may be NULL
   float* part_o;
   float2* part_ml;
-  int max_q, max_kv, window, sinks, nsplit;
+  int max_q, window, sinks, nsplit;
 };
 // Which kernel computes a call and how far it is split over the keys.
 enum Path { kDecode, kPrefill };

@@ -280,7 +280,7 @@ dd_status dd_paged_attn(const dd_paged_shape* shape, const dd_paged_seqs* seqs, 
   const AttnArgs a{q, q_stride * d.elt, out, lse_out,
                    p.merged ? reinterpret_cast<float*>(ws) : nullptr,
                    p.merged ? reinterpret_cast<float2*>(ws + w.ml) : nullptr, max_q_len,
-                   max_kv_len, window, sinks, p.nsplit};
+                   window, sinks, p.nsplit};
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = p.path == paged::kPrefill ? launch_attn_prefill(d, s, a, cs)
                                             : launch_attn_decode(d, s, a, cs);
