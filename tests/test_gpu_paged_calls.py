@@ -192,3 +192,51 @@ def test_bf16_keys_of_logit_minus_infinity_have_no_weight(d, tokens, most):
         c.table[b, i] = -1
     check_attention(c, out, lse)
     dd.check_device()
+
+
+@pytest.mark.parametrize("dtype,q4", [(BF, False), (BF, True), (F32, False)])
+@pytest.mark.parametrize("tokens", [1, 5, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_same_bits_beside_other_kernels(d, tokens, dtype, q4):
+    """Attention, reading and appending beside kernels that keep the load/store units busy."""
+    c = Cache([tokens] * 12, [tokens + 700 * b for b in range(12)], 16, 4, d, 64, dtype, q4)
+    count, T = 4000, c.n_tokens
+    seqs = c.seqs()
+    ws = torch.empty(max(16, dd.paged_attn_workspace_size(c.shape, T, tokens, 8000)),
+                     dtype=torch.uint8, device="cuda")
+    out, lse, q_out = torch.empty_like(c.q), torch.empty(T, 16, device="cuda"), torch.empty_like(c.q)
+    dense = [torch.empty(12, 4, count, d, dtype=dtype, device="cuda") for _ in range(2)]
+    k, v = (c.q[:, i:i + 4].contiguous() for i in (0, 4))
+    cs = torch.randn(8100, 2, d // 2, device="cuda")
+    results = [out, lse, q_out, *dense, *c.pools]
+    start = [p.clone() for p in c.pools]
+
+    def calls(stream=None):
+        dd.paged_append(c.shape, seqs, c.q, k, v, q_out, rope=cs, stream=stream)
+        dd.paged_attn(c.shape, seqs, q_out, out, lse, ws, max_q_len=tokens, max_kv_len=8000,
+                      stream=stream)
+        dd.paged_read(c.shape, seqs, 17, count, *dense, stream=stream)
+
+    calls()
+    torch.cuda.synchronize()
+    want = [x.view(torch.uint8).clone() for x in results]
+    a = torch.randn(1 << 22, device="cuda")
+    b = torch.empty_like(a)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream(priority=-1)
+    for _ in range(6):
+        for p, x in zip(c.pools, start):
+            p.copy_(x)
+        for x in results[:5]:
+            x.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(10):
+                torch.mul(a, 2.0, out=b)
+        calls(main)
+        with torch.cuda.stream(side):
+            for _ in range(10):
+                torch.mul(a, 2.0, out=b)
+        torch.cuda.synchronize()
+        for got, x in zip(results, want):
+            assert torch.equal(got.view(torch.uint8), x)
+    dd.check_device()
