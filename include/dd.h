@@ -480,9 +480,9 @@ dd_status dd_paged_pool_bytes(const dd_paged_shape* shape, size_t* bytes);
  * sum rounded to fp32, then to dtype.  4-bit pages take the rotated bf16 keys
  * (and the values) in groups of 32: m = the lowest, s = bf16((highest - m) /
  * 15), c = round((x - m) / s) to the nearest, ties to even, within 0 .. 15
- * (0 where s is 0).  A group that holds an infinity or NaN has no meaningful
- * codes.  A token whose position is negative or, with rope, not below
- * rope_len is skipped: nothing is written for it.
+ * (0 where s is 0).  A group that holds an infinity or NaN, or whose highest - m
+ * is beyond fp32, has no meaningful codes.  A token whose position is negative or,
+ * with rope, not below rope_len is skipped: nothing is written for it.
  */
 dd_status dd_paged_append(const dd_paged_shape* shape, const dd_paged_seqs* seqs,
                           int32_t n_tokens, const void* q, const void* k, const void* v,
@@ -522,7 +522,7 @@ dd_status dd_paged_read(const dd_paged_shape* shape, const dd_paged_seqs* seqs, 
  * workspace may be NULL); nothing in it has to be set or kept, and calls that
  * may run at the same time need one each.  Sums and the softmax are fp32; with
  * bf16 the weights exp(s_j - max) are rounded to bf16 for the product with V
- * where the tensor cores compute it.
+ * where the tensor cores compute it (over 4-bit pages also a weight times a step).
  * What the pages hold at positions that no token of the call's sequence sees
  * is without effect, whatever its bits.  An infinity or NaN at a position that
  * some token of a sequence sees may reach that sequence's other tokens too.

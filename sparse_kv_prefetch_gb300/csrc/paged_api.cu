@@ -54,7 +54,7 @@ Plan attn_plan(const Dims& d, int max_q, int max_kv, int window, int sinks) {
   Plan p;
   // At most 16 rows share a key: reading the keys bounds the call.  More: the
   // products do.  4-bit pages stay with the kernel for few rows up to 32, 16 at a
-  // time (4 x 5 tokens, 32 / 8 heads, over 65536 keys: 330 us against 364 on
+  // time (4 x 5 tokens, 32 / 8 heads, over 65536 keys: 330 to 350 us against 364 on
   // tcgen05, over 4000 keys 31 against 42; with 12 tokens 387 and 369; bf16 188
   // and 179), and fp32 always: its products do not run on tcgen05.  (On the CUDA
   // cores, 64 rows to a CTA, 2048 and 700 tokens took 1402 us with d = 128 and 691
@@ -62,19 +62,21 @@ Plan attn_plan(const Dims& d, int max_q, int max_kv, int window, int sinks) {
   // here 68 and 31.)
   const bool q4 = d.format == DD_PAGES_Q4;
   p.path = d.dtype == DD_F32 || rows <= (q4 ? 32 : 16) ? kDecode : kPrefill;
-  // How far the keys are split, by an estimate in ns from measured rates (bytes
-  // of keys and values a ns, d = 128, 32 query heads on 8 KV heads):
-  //   plain pages: the card's 6500, or a CTA's 64 where its share takes longer;
-  //   4-bit pages, which an SM's instructions bound: 21 an SM, 16 for a CTA alone
-  //     on one, the fullest SM counting;
+  // How far the keys are split, by an estimate in ns from rates (bytes of keys and
+  // values a ns) that were measured with d = 128 and 32 query heads on 8 KV heads,
+  // and are taken for the other shapes too:
+  //   plain pages: the card's 6500, or a CTA's 64 where its share takes longer (so
+  //     too for fp32 calls of many rows, which arithmetic bounds);
+  //   4-bit pages: 21 an SM, 16 for a CTA alone on one, the fullest SM counting;
   //   many rows a key: 13 ns a key for a CTA's 256 rows, 34 over 4-bit pages;
   //   a wave of CTAs takes 4000 more (8000 with many rows), a second kernel 5500
   //     and the partials.
   // Of the splits within 4 % of the cheapest the most: sequences are shorter than
-  // max_kv by their own measure, and many CTAs even them out.  Measured: 8 x
-  // 131072 keys, 4 splits (one cluster each) 500 us, 8 512, 19 510, 38 512, but 1
-  // of 8 sequences that long 263, 138, 90, 90; in 4 bits 480, 392, 352, 329; 32 x
-  // 4100 keys 97, 111, 108, 143, and unsplit 83.
+  // max_kv by their own measure, and many CTAs even them out.  Measured with the
+  // number given by hand: 8 x 131072 keys, 4 splits (one cluster each) 500 us, 8
+  // 512, 19 510, 38 512 (the rule takes 22), but 1 of 8 sequences that long 263,
+  // 138, 90, 90; in 4 bits 480, 392, 352, 329; 32 x 4100 keys 97, 111, 108, 143,
+  // and unsplit 83 (the rule leaves them whole).
   const bool decode = p.path == kDecode;
   const int cta_rows = p.path == kPrefill ? prefill_rows(d) : rows <= 8 ? 8 : 16;
   const long long at_once = (long long)kSms * (decode ? decode_ctas(d, rows <= 8 ? 1 : 2) : 1);

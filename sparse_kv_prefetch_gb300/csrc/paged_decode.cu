@@ -3,16 +3,17 @@
 //
 // The kernel is bound by reading every visible key and value once.  Up to 8 NR
 // rows ((token, query head of the group) pairs) share each row of the cache; a
-// call is split over the keys until the card is full, every CTA is four warps,
-// and every warp walks over its own tiles of 16 keys (a tile lies in one page)
-// with a ring of its own, filled by asynchronous 16-byte copies, and a softmax
-// of its own.  Nothing synchronises the warps before their results are merged.
+// call is split over the keys until the card is full, every CTA is four warps (six
+// for more than 8 fp32 rows of 512 bytes), and every warp walks over its own tiles
+// of 16 keys (a tile lies in one page) with a ring of its own, filled by
+// asynchronous 16-byte copies, and a softmax of its own.  Nothing synchronises the
+// warps before their results are merged.
 // Up to eight splits are a cluster, which merges them in its shared memory and
 // writes the result; more go through the workspace and a second kernel.
 // Measured (32 query heads on 8 KV heads, d = 128), of the bytes that have to be
-// read: bf16, 8 contexts of up to 131072 510 us, 7.1 TB/s (a copy reaches 6.8);
-// a window of 4096 over 32 requests 83 us, 6.5 TB/s; fp32, 4 contexts 494 us,
-// 6.1 TB/s.
+// read: bf16, 8 contexts of up to 131072 506 us, 7.2 TB/s (a copy reaches 6.8; the
+// short contexts stay in L2 between calls); a window of 4096 over 32 requests 80
+// us, 6.7 TB/s; fp32, 4 contexts of 92000 457 us, 6.6 TB/s.
 //
 // The products run on warp-level matrix instructions with the keys (then the
 // head's elements) as the 16 rows of A and the queries as the 8 columns of B:
@@ -33,10 +34,11 @@
 //         and rounded once, c - 8 is exact, and centring the codes keeps that
 //         rounding in proportion to the value; the last two are again one
 //         matrix instruction over the pairs.
-// These pages are bound by instructions, some 560 for a tile of 16 keys (the
-// integer pipe is 63 % busy, DRAM 44 %): 8 contexts of up to 131072 330 us,
-// 3.5 TB/s, two thirds of the bf16 pages' time.  Two tiles share the tests of one
-// (365 us without), and four CTAs of 128 threads share an SM.
+// 8 contexts of up to 131072 take 331 us, 3.4 TB/s, two thirds of the bf16 pages'
+// time: some 560 instructions for a tile of 16 keys.  No unit is full (issue slots
+// 64 %, the integer pipe 63 %, DRAM 44 %); what holds the rest up is not settled.
+// Two tiles share the tests of one (365 us without), and four CTAs of 128 threads
+// share an SM.
 //
 // fp32 pages: the same products on tf32 (11 bits of the mantissa) would lose
 // half the digits, so every operand is split into what tf32 holds and the rest,

@@ -11,7 +11,7 @@ namespace {
 
 // One CTA per (token, query head): the log-sum-exp merge of its partials.  The
 // warps take every fourth split each, so that many loads are in flight: 256 rows
-// of 19 splits 6.5 us.
+// of 22 splits 7.4 us, 25984 rows of 8 splits 38 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
     attn_merge_kernel(Seqs s, AttnArgs a, int Hq, long long rows) {

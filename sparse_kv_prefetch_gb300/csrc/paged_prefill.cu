@@ -24,25 +24,33 @@
 //
 // CTAs differ by their number of keys, and one fills an SM.  So a CTA goes on
 // with the work of CTAs that have not started (cluster launch control hands it
-// their places one at a time, the long ones first): the card stays full to the
-// end, and the next Q, K and V are on their way, and S is computed, while the
-// last rows are still being written.
+// their places one at a time): the card stays full to the end, and the next Q, K
+// and V are on their way, and S is computed, while the last rows are still being
+// written.  Places are handed out from the highest row tile of the grid down: of
+// prompts without a cached context that is the longest work first.  A sequence
+// with few new tokens has only low row tiles, so its places come last however
+// long its context is (a prompt of 2048 beside seven single tokens over 131072
+// keys takes 982 us, the two apart 44 and 527).
 //
 // Measured (32 query heads, d = 128): prompts of 8192 and 3001 tokens on 8 KV
-// heads 400 us, 1559 TFLOP/s (a bf16 matrix product of 8192 reaches 1939; before
-// the rows left through TMA, 416 us, and 382 of them with the exponentials left
-// out); of 8192 and 5000 with a window of 1024 on 32 KV heads 232 us, where a CTA
-// has some ten tiles of keys, half of them cut by the mask.  Issuing the products
-// from `lane == 0` instead of an elected thread took 570 and 339 us, and one CTA
-// to each place of the grid 441 and 279.
+// heads 400 us with pauses between calls, 1559 TFLOP/s (a bf16 matrix product of
+// 8192 reaches 1939), and 432 back to back, where power holds the clock; of 8192
+// and 5000 with a window of 1024 on 32 KV heads 231 and 237 us, where a CTA has
+// some ten tiles of keys, half of them cut by the mask.  With pauses, too: before
+// the rows left through TMA 416 us, and 382 of them with the exponentials left
+// out; issuing the products from `lane == 0` instead of an elected thread 570 and
+// 339 us, and one CTA to each place of the grid 441 and 279.  On 8 KV heads back to
+// back 337 us with d = 64, 1020 with d = 256.
 //
 // 4-bit pages: m + s c has more bits than a bf16, and rounding it would move
 // the logits by 2^-9 of their terms.  Four warps widen each tile of codes into
 // two bf16 tiles, the rounded values and what the rounding left (together good
 // to 2^-17), and every product is issued for both: twice the work on the tensor
 // cores, in tiles of 64 keys.  512 and 300 tokens over 32768 and 20011 positions
-// 672 us, 35 of them the merge of the splits; with the widening left out 623,
-// with only the first of the two products 703.
+// 673 us, 38 of them the merge of eight splits.  Neither the widening bounds it
+// (left out: 623 us) nor the products (the first of the two alone: 703): what is
+// left is the chain of one tile, S, a softmax of only 64 columns, P V, with a
+// barrier between each.
 #include <math.h>
 
 #include <type_traits>
