@@ -122,3 +122,31 @@ def test_sequences_of_several_turns_of_the_grid(form):
     c.poison(250, 3)
     out, lse, _ = call(c, 40, 900, 250, 3)
     check_attention(c, out, lse, 250, 3)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "-".join(map(str, f)))
+def test_prompts_on_two_streams_at_once(form):
+    """Two grids larger than the card beside each other, one of them split."""
+    heads, kv_heads, d, page, q4 = form
+    caches = [Cache(*mixed(45, 3), heads, kv_heads, d, page, BF, q4, seed=1),
+              Cache([300] * 6, [300, 2000, 999, 5000, 301, 777], heads, kv_heads, d, page, BF, q4)]
+    made = []
+    for c, most in zip(caches, (900, 20000)):
+        n = dd.paged_attn_workspace_size(c.shape, c.n_tokens, 300, most)
+        made.append((c, c.seqs(), torch.empty_like(c.q), torch.empty(c.q.shape[:2], device="cuda"),
+                     torch.empty(max(16, n), dtype=torch.uint8, device="cuda"), most))
+    want = []
+    for c, seqs, out, lse, ws, most in made:
+        dd.paged_attn(c.shape, seqs, c.q, out, lse, ws, max_q_len=300, max_kv_len=most)
+        check_attention(c, out, lse)
+        want.append((out.clone(), lse.clone()))
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (c, seqs, out, lse, ws, most) in zip(streams, made):
+            dd.paged_attn(c.shape, seqs, c.q, out, lse, ws, max_q_len=300, max_kv_len=most,
+                          stream=st)
+    torch.cuda.synchronize()
+    for (o, l), (_, _, out, lse, _, _) in zip(want, made):
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    dd.check_device()
