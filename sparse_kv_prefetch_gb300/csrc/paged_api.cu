@@ -51,6 +51,7 @@ dd_status resolve(const dd_paged_shape* s, Dims* o) {
 
 Plan attn_plan(const Dims& d, int max_q, int max_kv, int window, int sinks) {
   const long long rows = (long long)max_q * d.G;
+  max_kv = std::min(max_kv, 1 << 30);  // positions end there
   Plan p;
   // At most 16 rows share a key: reading the keys bounds the call.  More: the
   // products do.  4-bit pages stay with the kernel for few rows up to 32, 16 at a
@@ -121,7 +122,7 @@ Plan attn_plan(const Dims& d, int max_q, int max_kv, int window, int sinks) {
     }
     return std::max(tried[k], need);
   };
-  p.nsplit = split(std::min(max_kv, 1 << 30), kMaxSplits);  // positions end there
+  p.nsplit = split(max_kv, kMaxSplits);
   // A window leaves fewer keys; never more splits, for the workspace's sake.
   if (window > 0)
     p.nsplit = split(std::min((long long)max_kv, (long long)window + max_q + sinks), p.nsplit);

@@ -240,3 +240,12 @@ def test_the_same_bits_beside_other_kernels(d, tokens, dtype, q4):
         for got, x in zip(results, want):
             assert torch.equal(got.view(torch.uint8), x)
     dd.check_device()
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_the_widest_window_takes_no_more_workspace(tokens):
+    """The size asked for without a window serves any, at the largest values of everything."""
+    c = Cache([tokens, 1], [500, 77])
+    most = 2 ** 31 - 1
+    check_attention(c, *run_attention(c, most, most, max_kv=most), most, most)
+    check_attention(c, *run_attention(c, 2 ** 30, 2 ** 30, max_kv=most), 2 ** 30, 2 ** 30)
