@@ -279,7 +279,8 @@ __device__ __forceinline__ uint32_t piece_at(int r, int p) {
 // tf32), so there it becomes NaN.  A key and a row at a time; rows of D + 4 into po,
 // (max, sum) into pml.  Where the warp's keys lie is found again, so that the kernel
 // keeps no registers for it; as a function of its own it costs calls of many rows of
-// 512 bytes 3 % (1404 us without, 1450 with, 1506 inlined), others nothing.
+// 512 bytes 3 % (1404 us without, 1450 with, 1506 inlined), of 256 bytes 1 % (497,
+// 503 and 519), of few rows nothing.
 template <int D>
 __device__ __noinline__ void in_plain_fp32(Seqs s, AttnArgs a, int Hkv, int G, int warps,
                                            long long r0, int nr, float k1, float* po,

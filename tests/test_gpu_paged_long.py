@@ -1,5 +1,5 @@
-"""Attention over the most positions a table may have: one page, repeated, so that the result is a weighted
-mean of its rows with counts for weights."""
+"""Attention over the most positions a table may have: one page, repeated, so that the result
+is a weighted mean of its rows with counts for weights."""
 import pytest
 import torch
 
